@@ -15,11 +15,10 @@
 // e4m3.  S is formed from the cache's 8-bit values (kind::f8f6f4, fp32 accumulation,
 // exact products): Q, scaled by a power of two per row, is the exact sum of two e4m3
 // terms, each multiplied in turn, and the keys' scales multiply the scores.  For few
-// query rows P V is too: P as two terms keeps about 9 bits, as bf16 would, and the
-// values' scales s_v enter the exponent: P' = 2^(s + log2 s_v - m) with m following
-// the maximum of that sum, so that a row's largest *contribution* sits at
-// 2^6 .. 2^8.75 of the e4m3 range whatever the scales are (two-term values keep their
-// bits down to 2^-6); l sums P' / s_v.  For more rows P is f16 and V is scaled and
+// query rows P V is too: P as three e5m2 terms keeps 8 to 9 bits, and the values' scales s_v
+// enter the exponent: P' = 2^(s + log2 s_v - m) with m following the maximum of that
+// sum, so that a row's largest *contribution* sits at 2^13 .. 2^15.75 of the terms'
+// range whatever the scales are; l sums P' / s_v.  For more rows P is f16 and V is scaled and
 // converted to f16 on its way.
 //
 // Rows behind the sequence and drafted tokens that a query row does not see may
@@ -308,9 +307,9 @@ __device__ __forceinline__ void mma8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::f8f6f4 with A and B e4m3 (format 0), D fp32.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+// Instruction descriptor, kind::f8f6f4 with A and B e4m3 (format 0; b5: B e5m2), D fp32.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn, bool b5 = false) {
+  return (1u << 4) | ((b5 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Instruction descriptor of kind::f16 for f16 x f16 -> fp32.
@@ -336,7 +335,7 @@ __device__ __forceinline__ bool barrier_any(int id, int n, bool mine) {
   return any != 0;
 }
 
-// A K or V tile of 128 keys in shared memory, and the exponent range of P.
+// A K or V tile of 128 keys in shared memory.
 template <int kD, bool kE4m3>
 struct CacheTile {
   static constexpr int D = kD;
@@ -345,11 +344,6 @@ struct CacheTile {
   static constexpr int kChunks = kRowBytes > 128 ? 2 : 1;  // 128-byte columns of a tile
   static constexpr int kChunkRow = kRowBytes / kChunks;    // 64 or 128 bytes
   static constexpr int kChunkBytes = kTileBytes / kChunks;
-  // exponent of a row's largest weight when its reference is set, and how far
-  // above that it may grow before the reference is set anew: 2^8 (bf16), 2^8.75
-  // = 430 < 448 (e4m3)
-  static constexpr float kTop = kE4m3 ? 6.f : 0.f;
-  static constexpr float kGrow = kE4m3 ? 2.75f : 8.f;
 };
 
 struct CacheMaps {
@@ -500,14 +494,26 @@ __device__ __forceinline__ KeyFactors key_factors(float2 scales, float scale_log
   return KeyFactors{scales.x * scale_log2, __log2f(s), __frcp_rn(s)};  // 2^-22 is enough
 }
 
-// Two values up to 448 as two e4m3 terms each (f16 in between: 11 bits hold both);
-// the low byte is x's.
-__device__ __forceinline__ void split_p(float2 p, uint32_t* hi, uint32_t* lo) {
-  const __half2 ph = __floats2half2_rn(p.x, p.y);
-  const __nv_fp8x2_storage_t e0 = __nv_cvt_halfraw2_to_fp8x2(ph, __NV_SATFINITE, __NV_E4M3);
-  const __half2 rest = __hsub2(ph, __half2(__nv_cvt_fp8x2_to_halfraw2(e0, __NV_E4M3)));
-  *hi = e0;
-  *lo = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+// Two f16 as e4m3, and back.
+__device__ __forceinline__ uint32_t e4m3_of(__half2 x) {
+  return __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 half_of(uint32_t e) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e, __NV_E4M3));
+}
+// Two weights (f16, below 2^15.8) as three e5m2 terms each, in bytes 1 and 3 of t: e5m2
+// is the upper byte of f16, so a term is cut off and the rest, exact, goes on; the last
+// is rounded.  The sum is within 2^-8.6 of the weight, or 2^-17, that is 2^-30 of the
+// row's largest (kTop).  (Two e4m3 terms dropped what was below 2^-16 of it: next
+// to one key of weight 2^16, 28000 of 1 left O 14 % off.  Three cost conversions: 16
+// rows 7 % longer.)
+__device__ __forceinline__ void split_p(uint32_t x, uint32_t* t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    t[i] = x & 0xff00ff00u;
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(x) : "r"(t[i]));
+  }
+  t[2] = x + 0x00800080u;  // NaN (0x7fff) carries nowhere
 }
 
 // Splits 8 elements of a Q row (kLanes lanes hold the row) into two e4m3 terms
@@ -534,9 +540,12 @@ __device__ __noinline__ SplitQ split_q(uint4 v) {
   const float up = __uint_as_float((uint32_t)(127 + k) << 23);
   uint32_t hi[4], lo[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    split_p(make_float2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up),
-            &hi[i], &lo[i]);
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * up,
+                                        __uint_as_float(w[i] & 0xffff0000u) * up);
+    hi[i] = e4m3_of(x);
+    lo[i] = e4m3_of(__hsub2(x, half_of(hi[i])));
+  }
   return SplitQ{make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16),
                 __uint_as_float(bits < 0x7f80 ? (uint32_t)(127 - k) << 23 : 0x7fc00000u)};

@@ -24,8 +24,8 @@
 // shared memory), the references raised and the accumulator's columns rescaled.  A
 // row that has seen no key yet has reference -1e30 (kept negated): its first
 // visible key raises it.
-// P goes to shared memory (keys contiguous: the B operand), one element (e4m3:
-// one byte of each of two terms) per thread and row.
+// P goes to shared memory (keys contiguous: the B operand), one element (e4m3: three
+// terms, two keys' bytes of each) per thread and row.
 // At the end of a piece each group leaves its m and l in shared memory, and the
 // group of the last tile joins the accumulators of all; the others go on with the
 // next piece (statistics and accumulators are double-buffered by piece).
@@ -49,12 +49,13 @@ namespace fa {
 template <int kD, bool kE4m3, int kR>
 struct CacheKeysCfg : CacheTile<kD, kE4m3> {
   using T = CacheTile<kD, kE4m3>;
-  // columns of S^T and O^T: the rows (at least the 16 of an MMA), or two e4m3
-  // terms of each
+  // columns of S^T: the rows (at least the 16 of an MMA), or two e4m3 terms of each;
+  // of O^T: the same, or three e5m2 terms (24 make it 32: a multiple of 16)
   static constexpr int kN = kE4m3 ? 2 * kR : (kR < 16 ? 16 : kR);
+  static constexpr int kNO = kE4m3 ? (3 * kR + 15) / 16 * 16 : kN;
   static constexpr int kQBytes = kN * T::kRowBytes < 1024 ? 1024 : kN * T::kRowBytes;
   static constexpr int kPRow = kE4m3 ? 128 : 256;  // bytes of a row of P: 128 keys
-  static constexpr int kPBytes = kN * kPRow;
+  static constexpr int kPBytes = kNO * kPRow;
   // softmax groups: bf16 tiles of d = 128 take the memory longer than one group
   // takes for two
   static constexpr int kG = kR <= 16 && T::kTileBytes < 32768 ? 4 : 2;
@@ -71,11 +72,16 @@ struct CacheKeysCfg : CacheTile<kD, kE4m3> {
   static constexpr int kSmem = kOffV + kVStages * T::kTileBytes + 1024;  // + alignment slack
   static constexpr int kTmemCols = 512;
   // scores of group e at kN e; accumulator of group e in pieces of parity y at
-  // kColO + kN (e + kG y)
-  static constexpr uint32_t kColS = 0, kColO = 256;
+  // kColO + kNO (e + kG y)
+  static constexpr uint32_t kColS = 0, kColO = 128;
+  // exponent of a row's largest weight when its reference is set, and how far above
+  // that it may grow before the reference is set anew: 2^8 (bf16), 2^15.75 = 55000 of
+  // e5m2's 57344
+  static constexpr float kTop = kE4m3 ? 13.f : 0.f;
+  static constexpr float kGrow = kE4m3 ? 2.75f : 8.f;
   static constexpr int kProducerWarp = 4 * kG;  // the first of four
   static constexpr int kThreads = 32 * (kProducerWarp + 4);
-  static_assert(kN * kG <= 256 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "");
+  static_assert(kN * kG <= 128 && 2 * kNO * kG <= 384 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "");
 };
 
 constexpr float kUnset = 1e30f;  // negated reference of a row that has seen no key
@@ -145,17 +151,17 @@ __device__ __noinline__ void issue_values(uint32_t tO, uint32_t v, uint32_t pb, 
   tc_fence_after();
   const uint64_t dp = sdesc_sw128(pb, 16, 1024);
   if constexpr (kE4m3) {
-    constexpr uint32_t idesc = idesc_e4m3(128, C::kN, true, false);
+    constexpr uint32_t idesc = idesc_e4m3(128, C::kNO, true, false, true);
     const uint64_t dv = C::D == 64 ? sdesc_sw64(v, 0) : sdesc_sw128(v, 1024, 1024);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)  // 32 keys each
       mma8_ss(tO, dv + ((32 * C::kRowBytes * ks) >> 4), dp + 2 * ks, idesc, ks > 0 ? 1u : accumulate);
   } else {
-    constexpr uint32_t idesc = idesc_bf16(128, C::kN, true, false);
+    constexpr uint32_t idesc = idesc_bf16(128, C::kNO, true, false);
     const uint64_t dv = sdesc_sw128(v, C::D == 64 ? 0 : C::kChunkBytes, 1024);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)  // 16 keys each
-      mma_ss(tO, dv + 128 * ks, dp + (((ks >> 2) * C::kN * 128 + (ks & 3) * 32) >> 4), idesc,
+      mma_ss(tO, dv + 128 * ks, dp + (((ks >> 2) * C::kNO * 128 + (ks & 3) * 32) >> 4), idesc,
              ks > 0 ? 1u : accumulate);
   }
   mma_commit(done);
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
     }
     for (int piece = 0; more; ++piece) {
       const int y = piece & 1;
-      const uint32_t tO = tmem + C::kColO + C::kN * (e + kG * y);
+      const uint32_t tO = tmem + C::kColO + C::kNO * (e + kG * y);
       const int tiles = w.t1 - w.t0;
       if (wq == 0 && lane < kR) s_nm[e][lane] = lane < w.rows ? kUnset : -INFINITY;  // unused: weight 0
       // the statistics, flags and accumulators of the piece before last are free
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < C::kN; c += 16) {
+              for (int c = 0; c < C::kNO; c += 16) {
                 uint32_t o[16];
                 FA_TMEM_LD16_SYNC(tO + lane_off + c, o);
 #pragma unroll
@@ -478,24 +484,39 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
         if (ok && n >= kG) ok = __all_sync(0xffffffffu, values_done(n - kG));
         uint8_t* const pb = smem + C::kOffP + e * C::kPBytes;
         if constexpr (kE4m3) {
-          uint8_t* const at = pb + (kk & 15);
-          const uint32_t c16 = kk >> 4;
+          // Neighbouring keys exchange rows, so that a store has both keys' bytes of a row
+          // (by one byte the stores took 5 % of a call with 16 rows): the even lane takes
+          // rows 4 j and 4 j + 1, the odd one 4 j + 2 and 4 j + 3, in other banks.
+          const int odd = lane & 1;
+          uint8_t* const at = pb + (kk & 14) + odd * 256;
+          const uint32_t c16 = (kk >> 4) ^ (2 * odd);
+          const uint32_t sel0 = odd ? 0x1054 : 0x5410, sel1 = odd ? 0x3276 : 0x7632;
 #pragma unroll
-          for (int r = 0; r < kR; r += 2) {
-            const float2 nm = *reinterpret_cast<const float2*>(&s_nm[e][r]);
-            const float2 z = add2(make_float2(t[r], t[r + 1]), nm);
-            const float2 pv = make_float2(ex2(z.x), ex2(z.y));
-            const float2 sum = fma2(pv, make_float2(inv, inv), make_float2(l[r], l[r + 1]));
-            l[r] = sum.x;
-            l[r + 1] = sum.y;
-            uint32_t hi, lo;
-            split_p(pv, &hi, &lo);
-            uint8_t* const a0 = at + r * 128 + ((c16 ^ (r & 7)) << 4);
-            uint8_t* const a1 = at + (r + 1) * 128 + ((c16 ^ ((r + 1) & 7)) << 4);
-            a0[0] = (uint8_t)hi;
-            a1[0] = (uint8_t)(hi >> 8);
-            a0[kR * 128] = (uint8_t)lo;  // kR is a multiple of 8: the same swizzle
-            a1[kR * 128] = (uint8_t)(lo >> 8);
+          for (int r = 0; r < kR; r += 4) {
+            uint32_t x[2];  // rows r, r + 1; r + 2, r + 3 as f16
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int i = r + 2 * j;
+              const float2 nm = *reinterpret_cast<const float2*>(&s_nm[e][i]);
+              const float2 z = add2(make_float2(t[i], t[i + 1]), nm);
+              const float2 pv = make_float2(ex2(z.x), ex2(z.y));
+              const float2 sum = fma2(pv, make_float2(inv, inv), make_float2(l[i], l[i + 1]));
+              l[i] = sum.x;
+              l[i + 1] = sum.y;
+              x[j] = pack_f16(pv.x, pv.y);
+            }
+            const uint32_t mine = odd ? x[1] : x[0];
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t term[3];
+              split_p(__byte_perm(mine, other, j ? sel1 : sel0), term);
+              uint8_t* const a0 = at + (r + j) * 128 + ((c16 ^ ((r + j) & 7)) << 4);
+#pragma unroll
+              for (int i = 0; i < 3; ++i)  // kR is a multiple of 8: the same swizzle
+                *reinterpret_cast<uint16_t*>(a0 + i * kR * 128) =
+                    (uint16_t)__byte_perm(term[i], 0, 0x31);
+            }
           }
         } else {
           uint8_t* const at = pb + (kk >> 6) * C::kN * 128 + (kk & 7) * 2;
@@ -593,7 +614,7 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
         asm volatile("bar.sync %0, 128;" ::"r"(2 + e) : "memory");
         // lane kk of O^T holds element kk of every row
         if (ok && (C::D == 128 || wq < 2)) {
-          const uint32_t tall = tmem + C::kColO + C::kN * kG * y + lane_off;
+          const uint32_t tall = tmem + C::kColO + C::kNO * kG * y + lane_off;
 #pragma unroll 1
           for (int r0 = 0; r0 < last.rows; r0 += 8) {
             __syncwarp();  // the loads below are warp-wide
@@ -604,13 +625,15 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
             for (int g = 0; g < kG; ++g) {
               if (!has(g)) continue;
               uint32_t a[8];
-              FA_TMEM_LD8_SYNC(tall + C::kN * g + r0, a);
+              FA_TMEM_LD8_SYNC(tall + C::kNO * g + r0, a);
               if constexpr (kE4m3) {
-                uint32_t b[8];
-                FA_TMEM_LD8_SYNC(tall + C::kN * g + kR + r0, b);
+                uint32_t b[8], c[8];
+                FA_TMEM_LD8_SYNC(tall + C::kNO * g + kR + r0, b);
+                FA_TMEM_LD8_SYNC(tall + C::kNO * g + 2 * kR + r0, c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  o[j] = fmaf(__uint_as_float(a[j]) + __uint_as_float(b[j]), s_w[y][g][r0 + j], o[j]);
+                  o[j] = fmaf(__uint_as_float(a[j]) + (__uint_as_float(b[j]) + __uint_as_float(c[j])),
+                              s_w[y][g][r0 + j], o[j]);
               } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = fmaf(__uint_as_float(a[j]), s_w[y][g][r0 + j], o[j]);

@@ -81,7 +81,9 @@ struct CacheRowsCfg : CacheTile<kD, kE4m3> {
   // behind them, and 128 registers.
   static constexpr int kLastWarp = 11, kConvertWarp = 12;
   static constexpr int kThreads = kE4m3 ? 512 : 384;
-  // f16 weights reach 2^14 before a row's reference is set anew
+  // exponent of a row's largest weight when its reference is set, and how far above
+  // that it may grow before the reference is set anew: f16 weights reach 2^14
+  static constexpr float kTop = kE4m3 ? 6.f : 0.f;
   static constexpr float kGrow = 8.f;
   static_assert(2 * 128 * kD <= kQBytes, "Q fits its region");
 };

@@ -1,0 +1,65 @@
+"""Attention over an e4m3 cache where its roundings show: weights far below the largest,
+queries of uneven channels, value scales far apart.  Bounds are derived at each test; p are
+the weights (they sum to 1), v the values, sv the values' scales.  Every output is rounded
+(2^-8 of it), and so is every weight (2^-8)."""
+import math
+
+import pytest
+import torch
+
+import _cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+def _table(B, pages):
+    """Every sequence reads the same pages."""
+    return torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+
+
+def _attend64(c, q, k, v, kv_scales, sees=None):
+    """(o, p @ |v|, max(p sv) per row) in 64 bits of rows q [R, d] over k, v [n, d] (bytes) with
+    scales (ks, vs) [n]; sees: bool [R, n]."""
+    k, v = (x.float().cpu().to(F64) for x in (k, v))
+    ks, vs = (x.cpu().to(F64) for x in kv_scales)
+    s = (q.float().cpu().to(F64) @ k.T) * ks * c
+    if sees is not None:
+        s = s.masked_fill(~sees, -math.inf)
+    p = s.softmax(-1)
+    pv = p * vs
+    return pv @ v, pv @ v.abs(), pv.amax(-1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 8, 13, 16, 24])
+@pytest.mark.parametrize("n,w,spread", [(1 << 13, 14, 0.0), (28000, 16, 0.0), (28000, 16, 1.0),
+                                        (1 << 16, 17, 0.5), (1 << 17, 18, 0.0), (1 << 17, 20, 0.0)])
+def test_a_dominant_key_and_a_long_tail(fa, d, G, n, w, spread):
+    """One key at 0 and n keys of 2^-w of its weight and less; as many sequences as SMs, so that
+    none is cut and one CTA walks all keys.  Beside its rounding a weight may be off by 2^-29 of
+    the row's largest (weight times value scale): n of them."""
+    B, page = 152, 256
+    rows = -(-(n + 1) // page) * page
+    g = torch.Generator().manual_seed(60)
+    k = torch.zeros(rows, d)
+    k[1:n + 1, 0] = -1.0
+    v = (1.0 + 0.25 * torch.randn(rows, d, generator=g)) * 100
+    v[0] = 30 * torch.randn(d, generator=g)
+    ks = torch.full((rows,), float(w)) + spread * torch.rand(rows, generator=g)
+    vs = torch.full((rows,), 0.01)
+    lay = lambda x: x.view(rows // page, 1, page, *x.shape[1:])
+    k, v = (x.clamp(-448, 448).to(ref.F8).cuda() for x in (k, v))
+    ks, vs = ks.cuda(), vs.cuda()
+    cache = fa.KVCache(lay(k), lay(v), lay(ks), lay(vs), _table(B, rows // page))
+    q = torch.zeros(B, G, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = math.log(2.0)
+    start = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    o, lse = fa.cache_forward(q, cache, start, scale=scale)
+    want, mag, top = _attend64(scale, q[0, :1, 0], k[:n + 1], v[:n + 1], (ks[:n + 1], vs[:n + 1]))
+    # the scores: the product's fp32 rounding, of 2^6 at most
+    tol = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -16) * mag
+           + n * 2.0 ** -29 * top[:, None] * v[:n + 1].float().abs().max().cpu())
+    err = (o[:, :, 0].cpu().to(F64) - want).abs()
+    assert (err <= tol).all(), (float(err.max()), float((err / want.abs()).max()), float((err / tol).max()))
