@@ -13,8 +13,9 @@
 // same bit for bit from run to run.
 //
 // e4m3.  S is formed from the cache's 8-bit values (kind::f8f6f4, fp32 accumulation,
-// exact products): Q, scaled by a power of two per row, is the exact sum of two e4m3
-// terms, each multiplied in turn, and the keys' scales multiply the scores.  For few
+// exact products): Q, scaled by a power of two per row, is the sum of two 8-bit terms,
+// exact down to 2^-13 of the row's largest element, and the keys' scales multiply the
+// scores.  For few
 // query rows P V is too: P as three e5m2 terms keeps 8 to 9 bits, and the values' scales s_v
 // enter the exponent: P' = 2^(s + log2 s_v - m) with m following the maximum of that
 // sum, so that a row's largest *contribution* sits at 2^13 .. 2^15.75 of the terms'
@@ -307,9 +308,10 @@ __device__ __forceinline__ void mma8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::f8f6f4 with A and B e4m3 (format 0; b5: B e5m2), D fp32.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn, bool b5 = false) {
-  return (1u << 4) | ((b5 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+// Instruction descriptor, kind::f8f6f4 with A and B e4m3 (format 0; a5, b5: e5m2), D fp32.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn, bool a5 = false,
+                                                  bool b5 = false) {
+  return (1u << 4) | ((a5 ? 1u : 0u) << 7) | ((b5 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Instruction descriptor of kind::f16 for f16 x f16 -> fp32.
@@ -516,16 +518,20 @@ __device__ __forceinline__ void split_p(uint32_t x, uint32_t* t) {
   t[2] = x + 0x00800080u;  // NaN (0x7fff) carries nowhere
 }
 
-// Splits 8 elements of a Q row (kLanes lanes hold the row) into two e4m3 terms
-// of the row times 2^k; factor: 2^-k.  2^k is the largest power of two that
-// keeps the row within 448 = 1.75 2^8: the terms' sum is then exact (bf16 has 8
-// bits) down to 2^-10 of the scaled units.  A row with infinities or NaN has no
-// finite score: its factor is NaN.  Called by the whole warp.
+// Splits 8 elements of a Q row (kLanes lanes hold the row) into two terms of the row
+// times 2^k; factor: 2^-k.  2^k is the largest power of two that keeps the row within
+// 448 = 1.75 2^8.  The first term is e4m3.  What it leaves has three bits where it is
+// normal (2^-6 and up); the second term holds it as e5m2, where the terms' products add
+// up in one accumulator, or times 16 as e4m3 (kTimes16), where they are apart.  Either
+// way the sum is exact from 2^-6 up, 2^-13 of the row's largest (224 to 448), and at
+// most 2^-14 off below.  (With a second term of the first's type and scale 2^-10: rows with one
+// channel 1000 times the others lost bits of those.)  A row with infinities or NaN has
+// no finite score: its factor is NaN.  Called by the whole warp.
 struct SplitQ {
   uint2 hi, lo;
   float factor;
 };
-template <int kLanes>
+template <int kLanes, bool kTimes16>
 __device__ __noinline__ SplitQ split_q(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   // magnitudes compare as integers; infinities and NaN are the largest
@@ -544,7 +550,9 @@ __device__ __noinline__ SplitQ split_q(uint4 v) {
     const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * up,
                                         __uint_as_float(w[i] & 0xffff0000u) * up);
     hi[i] = e4m3_of(x);
-    lo[i] = e4m3_of(__hsub2(x, half_of(hi[i])));
+    const __half2 rest = __hsub2(x, half_of(hi[i]));
+    lo[i] = kTimes16 ? e4m3_of(__hmul2(rest, __float2half2_rn(16.f)))
+                     : __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E5M2);
   }
   return SplitQ{make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16),
                 make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16),

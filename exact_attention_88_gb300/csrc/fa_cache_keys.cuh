@@ -151,7 +151,7 @@ __device__ __noinline__ void issue_values(uint32_t tO, uint32_t v, uint32_t pb, 
   tc_fence_after();
   const uint64_t dp = sdesc_sw128(pb, 16, 1024);
   if constexpr (kE4m3) {
-    constexpr uint32_t idesc = idesc_e4m3(128, C::kNO, true, false, true);
+    constexpr uint32_t idesc = idesc_e4m3(128, C::kNO, true, false, false, true);
     const uint64_t dv = C::D == 64 ? sdesc_sw64(v, 0) : sdesc_sw128(v, 1024, 1024);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)  // 32 keys each
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
       for (int i = 0; i < kLoads; ++i) {
         const int r = (4 * i + pw) * kPer + sub;
         if constexpr (kE4m3) {
-          const SplitQ f = split_q<kLanes>(q8[i]);
+          const SplitQ f = split_q<kLanes, true>(q8[i]);
           if (r < kR) {
             *reinterpret_cast<uint2*>(q + e4m3_row_offset<C::D>(r, c8)) = f.hi;
             *reinterpret_cast<uint2*>(q + e4m3_row_offset<C::D>(kR + r, c8)) = f.lo;
@@ -385,14 +385,16 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
             page = key_page(p.c, w, key + 256 * kG);
             inv = f.inv;
             const float2 a2 = make_float2(f.score, f.score), b2 = make_float2(f.log2v, f.log2v);
+            const float2 sixteenth = make_float2(0.0625f, 0.0625f);
 #pragma unroll
             for (int r = 0; r < kR; r += 4) {
               const float4 rf = *reinterpret_cast<const float4*>(&s_rowf[y][kE4m3 ? r : 0]);
 #pragma unroll
               for (int j = 0; j < 4; j += 2) {
-                const float2 sum = add2(make_float2(__uint_as_float(s[r + j]), __uint_as_float(s[r + j + 1])),
-                                        make_float2(__uint_as_float(s[(C::kN / 2 + r + j) % C::kN]),
-                                                    __uint_as_float(s[(C::kN / 2 + r + j + 1) % C::kN])));
+                const float2 sum = fma2(make_float2(__uint_as_float(s[(C::kN / 2 + r + j) % C::kN]),
+                                                    __uint_as_float(s[(C::kN / 2 + r + j + 1) % C::kN])),
+                                        sixteenth,
+                                        make_float2(__uint_as_float(s[r + j]), __uint_as_float(s[r + j + 1])));
                 const float2 z = fma2(sum, mul2(a2, j ? make_float2(rf.z, rf.w) : make_float2(rf.x, rf.y)), b2);
                 t[r + j] = z.x;
                 t[r + j + 1] = z.y;

@@ -18,7 +18,7 @@
 // A tile takes about 1600 cycles (bf16, 61-token trees: 105 us, 56% of the memory's
 // rate), the chain of a tile's scores, exponentials and products.
 //
-// e4m3: S from the bytes themselves, Q as two e4m3 terms.  P and V are f16: four more
+// e4m3: S from the bytes themselves, Q as an e4m3 and an e5m2 term.  P and V are f16: four more
 // warps scale and convert V on its way, into two buffers of its own.  Its scales are
 // taken relative to 2^k, the power of two below the tile's largest, and 2^k enters the
 // exponents; what that costs is an absolute 2^-40 of the tile's largest value.  A
@@ -62,8 +62,8 @@ struct CacheRowsCfg : CacheTile<kD, kE4m3> {
   static constexpr int kKStages = kE4m3 ? 65536 / T::kTileBytes : kD == 128 ? 3 : 5;
   static constexpr int kVStages = kE4m3 ? 32768 / T::kTileBytes : kD == 128 ? 2 : 5;
   static constexpr int kV16Bytes = 256 * kD;  // a V tile as f16
-  // Q: 128 rows of bf16, or of two e4m3 terms; the epilogue joins lane blocks in it
-  static constexpr int kQTerm = 128 * kD;  // bytes of one e4m3 term
+  // Q: 128 rows of bf16, or of two 8-bit terms; the epilogue joins lane blocks in it
+  static constexpr int kQTerm = 128 * kD;  // bytes of one 8-bit term
   static constexpr int kOffQ = 0;
   static constexpr int kQBytes = 32768;
   static constexpr int kOffK = kQBytes;
@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
           tc_fence_after();
           const uint32_t k = sK + st * C::kTileBytes, tS = tmem + C::kColS + 128 * x;
           if constexpr (kE4m3) {
-            constexpr uint32_t idesc = idesc_e4m3(128, 128, false, false);
 #pragma unroll
-            for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t idesc = idesc_e4m3(128, 128, false, false, term > 0);
 #pragma unroll
               for (int ks = 0; ks < C::D / 32; ++ks) {
                 const uint32_t a = sQ + term * C::kQTerm + 32 * ks, b = k + 32 * ks;
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
                         C::D == 64 ? sdesc_sw64(b) : sdesc_sw128(b, 16, 1024), idesc,
                         term + ks > 0 ? 1u : 0u);
               }
+            }
           } else {
             constexpr uint32_t idesc = idesc_bf16(128, 128, false, false);
             const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(k, 16, 1024);
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
           for (int i = 0; i < kSteps; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             uint8_t* const mine = stage + 4096 * (i % kAhead);
-            const SplitQ f = split_q<kLanes>(*reinterpret_cast<const uint4*>(mine));
+            const SplitQ f = split_q<kLanes, false>(*reinterpret_cast<const uint4*>(mine));
             if (i + kAhead < kSteps) q_copy(i + kAhead, mine);  // read by this thread alone
             asm volatile("cp.async.commit_group;" ::: "memory");
             const int r = q_row(i);

@@ -63,3 +63,43 @@ def test_a_dominant_key_and_a_long_tail(fa, d, G, n, w, spread):
            + n * 2.0 ** -29 * top[:, None] * v[:n + 1].float().abs().max().cpu())
     err = (o[:, :, 0].cpu().to(F64) - want).abs()
     assert (err <= tol).all(), (float(err.max()), float((err / want.abs()).max()), float((err / tol).max()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 8), (1, 16), (1, 32), (5, 8), (20, 4), (16, 16)])
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 13])
+def test_queries_of_uneven_channels(fa, d, T, G, ratio):
+    """One channel of q is `ratio` times the others, and its entry is the same in every key, so
+    that the softmax does not see it; the others need all of bf16's bits and their errors would
+    add up.  q is exact down to 2^-13 of its row's largest element and at most 2^-21 of that off;
+    products are summed in fp32 (2^-21 d^(1/2) of sum |q k|, as in _cache_ref)."""
+    n = 600
+    c = ref.Cache(fa, 1, n + T, 1, d, 32, "e4m3", seed=62)
+    c.ks.fill_(2.0 ** -10)
+    c.vs.fill_(1.0 / 60)
+    g = torch.Generator().manual_seed(61)
+    sign = torch.where(torch.rand(c.k.shape[:3], generator=g) < 0.9, 1.0, -1.0)[..., None]
+    c.k.copy_((sign * 256).expand(*c.k.shape).to(ref.F8))
+    c.k[..., 5] = 2.0
+    q = torch.full((1, G, T, d), 0.50390625 * ratio / 1024)
+    q[..., 5] = ratio * torch.where(torch.rand(1, G, T, generator=g) < 0.5, 1.0, -1.0)
+    q = q.to(torch.bfloat16).cuda()
+    start = torch.tensor([n], dtype=torch.int32)
+    scale = 2.0 * 1024 / ratio / d
+    o, lse = fa.cache_forward(q, c.fa, start.cuda(), scale=scale)
+    raw = c.raw()
+    k, _ = c.rows(raw, 0, 0, 0, n + T)
+    v, _ = c.rows(raw, 1, 0, 0, n + T)
+    k, v = k[0], v[0]
+    for t in range(T):
+        kk, vv, qq = k[:n + t + 1], v[:n + t + 1], q[0, :, t].cpu().to(F64)
+        s = qq @ kk.T * scale
+        p = s.softmax(-1)
+        want, mag = p @ vv, p @ vv.abs()
+        ds = scale * (2.0 ** -21 * ratio * kk.abs().sum(-1).max()
+                      + 2.0 ** -21 * d ** 0.5 * (qq.abs() @ kk.abs().T).amax(-1))
+        el = (lse[0, :, t].cpu().to(F64) - s.logsumexp(-1)).abs()
+        assert (el <= ds + 2.0 ** -18).all(), (float(el.max()), float(ds.max()))
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * ds[:, None] + 2.0 ** -18) * mag + 2.0 ** -16 * mag
+        err = (o[0, :, t].cpu().to(F64) - want).abs()
+        assert (err <= tol).all(), (float((err / mag).max()), float((err / tol).max()))
