@@ -21,9 +21,11 @@
 // e4m3: S from the bytes themselves, Q as an e4m3 and an e5m2 term.  P and V are f16: four more
 // warps scale and convert V on its way, into two buffers of its own.  Its scales are
 // taken relative to 2^k, the power of two below the tile's largest, and 2^k enters the
-// exponents; what that costs is an absolute 2^-40 of the tile's largest value.  A
+// exponents; what that costs is an absolute 2^-40 of the tile's largest value.  (Tiles
+// with drafted rows: each key's scale stands in its own exponent, as in the other
+// kernel, and V is converted as it is.)  A
 // factor per key that every warp reads costs shared memory a cycle, so the softmax
-// reads one (the score's): 512 cycles a tile, next to the products' 770, the copies'
+// reads one (the score's; in those tiles three): 512 cycles a tile, next to the products' 770, the copies'
 // 256 and the conversion's 384; a tile takes 1900 to 2300.  With P as two e4m3 terms
 // and three factors per key (value scales in the exponents) it was 3600.  The loops are
 // kept short: with the conversion and the scales' loop unrolled, warps waited for
@@ -54,8 +56,9 @@ __device__ __forceinline__ void store_part(uint32_t taddr, const uint32_t* r, in
   }
 }
 
-template <int kD, bool kE4m3>
-struct CacheRowsCfg : CacheTile<kD, kE4m3> {
+template <int kD, bool kE4m3_>
+struct CacheRowsCfg : CacheTile<kD, kE4m3_> {
+  static constexpr bool kE4m3 = kE4m3_;
   using T = CacheTile<kD, kE4m3>;
   // 128 to 160 KB of K and V in flight or in use per SM: the SM's share of the
   // memory bandwidth (23 bytes a cycle) times about 2000 cycles needs 47 KB
@@ -88,21 +91,21 @@ struct CacheRowsCfg : CacheTile<kD, kE4m3> {
   static_assert(2 * 128 * kD <= kQBytes, "Q fits its region");
 };
 
-// Bits e of keys key0 + e, e < kKeys, that token t of the piece's sequence sees.
+// Bits e of keys key0 + e, e < kKeys, that token t of sequence b sees.
 template <int kKeys>
-__device__ __forceinline__ uint64_t visible_keys(const CacheFwdParams& p, const Piece& w, int t,
-                                                 int key0) {
+__device__ __forceinline__ uint64_t visible_keys(const CacheFwdParams& p, int b, int start, int klen,
+                                                 int t, int key0) {
   constexpr uint64_t kAll = kKeys == 64 ? ~0ull : (1ull << (kKeys & 63)) - 1;
-  const int n = w.klen - key0;
+  const int n = klen - key0;
   if (n <= 0) return 0;
   const uint64_t in = n >= kKeys ? kAll : (1ull << n) - 1;
-  const int pre = w.start - key0;  // keys of the sequence itself
+  const int pre = start - key0;  // keys of the sequence itself
   if (pre >= kKeys) return in;
   if (!p.mask) {
     const int last = pre + t;  // >= -kKeys... the last visible key
     return last < 0 ? 0 : last >= 63 ? in : in & ((2ull << last) - 1);
   }
-  const uint32_t* words = p.mask + ((long long)w.b * p.T + t) * p.W;
+  const uint32_t* words = p.mask + ((long long)b * p.T + t) * p.W;
   uint64_t bits;
   if (pre > 0) {
     const uint64_t lo = words[0], hi = p.W > 1 ? words[1] : 0;
@@ -118,6 +121,168 @@ __device__ __forceinline__ uint64_t visible_keys(const CacheFwdParams& p, const 
   return in & bits;
 }
 
+// What the softmax warps share of a tile.
+template <typename C, bool kE4m3>
+struct RowsShared {
+  // pv_done[h][x]: O_h has P_h V of buffer x's tile
+  uint64_t p_full[2][2], pv_done[2][2], v_full[C::kVStages], v16_full[2], scl_empty[2];
+  // per key of a tile: factor of its scores, value scale over 2^k (twice, as f16), and
+  // in a tile whose scales stand in the exponents (2^-k told as 0) their log2 and
+  // inverse; per tile: k, 2^-k
+  __align__(16) float scl[kE4m3 ? 2 : 1][4][kE4m3 ? 128 : 4];
+  float k[2][2];
+  int abort_flag, any_bad;
+  uint32_t bad[32];  // drafted rows with non-finite values (T <= 1024)
+};
+
+// The softmax of one tile whose scores are there: S(n) to P, m, l and, where m grows,
+// O_h.  token: of this thread's row, negative without one.  kSlow: an e4m3 tile with
+// drafted rows or the sequence's end.  False after a wait that gave up.
+template <typename C, bool kE4m3, int kRep, bool kSlow>
+__device__ __forceinline__ bool tile_step(const CacheFwdParams& p, int b, int start, int klen, bool first,
+                                          RowsShared<C, kE4m3>& sh, uint8_t* smem, int tile, int n,
+                                          uint32_t tmem, float rowf, int token, float& m, float& l) {
+  constexpr int kRows = 128 / kRep, kKeys = 64 / kRep;  // keys of a tile per softmax thread
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2, x = n & 1;
+  const int part = (threadIdx.x & 127) / kRows;  // warp-uniform
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t tO = tmem + C::kColO + C::D * h + lane_off;
+  const uint32_t tS = tmem + C::kColS + 128 * x + 64 * h + lane_off;
+  tc_fence_after();
+  uint32_t r[kKeys];
+  if constexpr (kKeys == 64) FA_TMEM_LD64_SYNC(tS, r);
+  if constexpr (kKeys == 32) FA_TMEM_LD32_SYNC(tS + 32 * part, r);
+  if constexpr (kKeys == 16) FA_TMEM_LD16_SYNC(tS + 16 * part, r);
+  const int koff = 64 * h + kKeys * part;  // the thread's keys in the tile
+  if constexpr (kE4m3) {
+#pragma unroll
+    for (int g = 0; g < kKeys; g += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(&sh.scl[kE4m3 ? x : 0][0][koff + g]);
+      float2 t0 = mul2(make_float2(__uint_as_float(r[g]), __uint_as_float(r[g + 1])), make_float2(a.x, a.y));
+      float2 t1 = mul2(make_float2(__uint_as_float(r[g + 2]), __uint_as_float(r[g + 3])), make_float2(a.z, a.w));
+      if constexpr (kSlow) {  // the value scales stand in the exponents
+        const float4 lv = *reinterpret_cast<const float4*>(&sh.scl[kE4m3 ? x : 0][2][koff + g]);
+        t0 = fma2(t0, make_float2(rowf, rowf), make_float2(lv.x, lv.y));
+        t1 = fma2(t1, make_float2(rowf, rowf), make_float2(lv.z, lv.w));
+      }
+      r[g] = __float_as_uint(t0.x);
+      r[g + 1] = __float_as_uint(t0.y);
+      r[g + 2] = __float_as_uint(t1.x);
+      r[g + 3] = __float_as_uint(t1.y);
+    }
+  }
+  if (kE4m3 ? kSlow : (tile + 1) * 128 > start) {  // drafted rows, and the sequence's end
+    const uint64_t vis = token >= 0 ? visible_keys<kKeys>(p, b, start, klen, token, tile * 128 + koff) : ~0ull;
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e)
+      if (!((vis >> e) & 1)) r[e] = 0xff800000u;
+    const int st = kE4m3 ? x : n % C::kVStages;
+    const bool ok = kE4m3 ? cache_wait_warp(&sh.v16_full[x], (n >> 1) & 1, &sh.abort_flag, p.status, 2524)
+               : cache_wait_warp(&sh.v_full[st], (n / C::kVStages) & 1, &sh.abort_flag, p.status, 2524);
+    if (!ok) return false;
+    const int row0 = 64 * h + 16 * (warp & 3);
+    if (tile * 128 + row0 + 16 > start)
+      clean_rows<C, false, kE4m3>(
+          smem + (kE4m3 ? C::kOffV16 + st * C::kV16Bytes : C::kOffV + st * C::kTileBytes), start, klen,
+          row0, row0 + 16, tile * 128, sh.bad, &sh.any_bad);
+  }
+  // the scale (positive) multiplies in the exponent; e4m3: the row's factor
+  const float exp_scale = !kE4m3 ? p.scale_log2 : kSlow ? 1.f : rowf;
+  const float k = kE4m3 && !kSlow ? sh.k[x][0] : 0.f;
+  float tmax = __uint_as_float(r[0]);
+  if constexpr (kKeys == 64) tmax = fmaxf(max32(r), max32(r + 32));
+  if constexpr (kKeys == 32) tmax = max32(r);
+  if constexpr (kKeys == 16) {
+#pragma unroll
+    for (int e = 1; e < 15; e += 2)
+      tmax = max3(tmax, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+    tmax = fmaxf(tmax, __uint_as_float(r[15]));
+  }
+  const float top = tmax * exp_scale + (k - C::kTop);
+  const bool grow = top > m + C::kGrow;  // true when m = -inf, top finite
+  float alpha = 1.f;
+  if (grow) {
+    alpha = (m == -INFINITY) ? 0.f : ex2(m - top);
+    m = top;
+  }
+  if (!first && __any_sync(0xffffffffu, grow)) {
+    // O_h holds the tiles before this one once the last P_h V is done
+    const bool ok = cache_wait_warp(&sh.pv_done[h][x ^ 1], ((n - 1) >> 1) & 1, &sh.abort_flag, p.status, 2525 + h);
+    if (!ok) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < C::D / 32; ++c) {
+      uint32_t o[32];
+      FA_TMEM_LD32_SYNC(tO + 32 * c, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      FA_TMEM_ST32(tO + 32 * c, o);
+    }
+  }
+  const float nm = (m == -INFINITY) ? 0.f : k - m;
+  const float2 c2 = make_float2(exp_scale, exp_scale), nm2 = make_float2(nm, nm);
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  // P rounded to bf16 (2^-8 of each weight), as in the forward kernels, or f16;
+  // signalling its first half early, as the d = 128 forward does, gained nothing here
+  uint32_t pk[kKeys / 2];
+#pragma unroll
+  for (int e = 0; e < kKeys; e += 4) {
+    float4 inv = make_float4(1.f, 1.f, 1.f, 1.f);
+    if constexpr (kE4m3 && kSlow)
+      inv = *reinterpret_cast<const float4*>(&sh.scl[kE4m3 ? x : 0][3][koff + e]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 s = make_float2(__uint_as_float(r[e + 2 * i]), __uint_as_float(r[e + 2 * i + 1]));
+      const float2 t = fma2(s, c2, nm2);
+      const float2 pv = make_float2(ex2(t.x), ex2(t.y));
+      if constexpr (kE4m3 && kSlow)
+        acc[i] = fma2(pv, i ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y), acc[i]);
+      else
+        acc[i] = add2(acc[i], pv);
+      pk[e / 2 + i] = kE4m3 ? pack_f16(pv.x, pv.y) : pack_bf16(pv.x, pv.y);
+    }
+  }
+  store_part<kKeys / 2, kRep>(tS, pk, part);
+  const float2 sum = add2(acc[0], acc[1]);
+  l = l * alpha + (sum.x + sum.y) * (kE4m3 && !kSlow ? sh.k[x][1] : 1.f);
+  tmem_wait_st();
+  tc_fence_before();
+  mbar_arrive_warp(&sh.p_full[x][h]);
+  if (kE4m3 && lane == 0) mbar_arrive(&sh.scl_empty[x]);
+  return true;
+}
+
+// The slow tiles' softmax, out of line: in the others' loop its code made long e4m3
+// calls 15 % longer.
+struct RowState {
+  float m, l;
+  bool ok;
+};
+template <typename C, int kRep>
+__device__ __noinline__ RowState slow_tile(const CacheFwdParams& p, int b, int start, int klen, bool first,
+                                           RowsShared<C, C::kE4m3>& sh, uint8_t* smem, int tile, int n,
+                                           uint32_t tmem, float rowf, int token, float m, float l) {
+  const bool ok = tile_step<C, C::kE4m3, kRep, C::kE4m3>(p, b, start, klen, first, sh, smem, tile, n, tmem,
+                                                         rowf, token, m, l);
+  return RowState{m, l, ok};
+}
+
+// The factors of four keys of a slow tile.
+static __device__ __noinline__ void slow_factors(float* at, float4 v) {
+  const float s[4] = {v.x, v.y, v.z, v.w};
+  float a[4], b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const KeyFactors f = key_factors(make_float2(0.f, s[e]), 0.f);
+    a[e] = f.log2v;
+    b[e] = f.inv;
+  }
+  const float one = __uint_as_float(0x3c003c00u);  // 1 twice, as f16
+  *reinterpret_cast<float4*>(at + 128) = make_float4(one, one, one, one);
+  *reinterpret_cast<float4*>(at + 256) = make_float4(a[0], a[1], a[2], a[3]);
+  *reinterpret_cast<float4*>(at + 384) = make_float4(b[0], b[1], b[2], b[3]);
+}
+
 template <int kD, bool kE4m3, int kRep, bool kPair>
 __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
     fa_cache_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -125,25 +290,24 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
   using C = CacheRowsCfg<kD, kE4m3>;
   constexpr int kRows = 128 / kRep;            // query rows of this CTA
   constexpr int kUnit = kPair ? 256 : kRows;   // of a unit
-  constexpr int kKeys = 64 / kRep;   // keys of a tile per softmax thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // pv_done[h][x]: O_h has P_h V of buffer x's tile.  A commit costs its thread some 200
+  // A commit costs its thread some 200
   // cycles, so barriers that tell the same are one: k_empty[st] is a tile's scores done,
   // pv_done[1] a V buffer free where there are two.
-  __shared__ uint64_t q_full, drain[2], p_full[2][2], pv_done[2][2];
-  __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages];
-  __shared__ uint64_t v_full[C::kVStages], v_empty[C::kVStages];
-  __shared__ uint64_t scl_full[2], scl_empty[2], v16_full[2];
+  __shared__ RowsShared<C, kE4m3> sh;
+  auto& p_full = sh.p_full;
+  auto& pv_done = sh.pv_done;
+  auto& v_full = sh.v_full;
+  auto& scl_empty = sh.scl_empty;
+  auto& v16_full = sh.v16_full;
+  auto& abort_flag = sh.abort_flag;
+  auto& s_scl = sh.scl;
+  __shared__ uint64_t q_full, drain[2], scl_full[2];
+  __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_empty[C::kVStages];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, any_bad;
-  __shared__ uint32_t bad[32];  // drafted rows with non-finite values (T <= 1024)
   __shared__ float s_m[2][128], s_l[2][128], s_rowf[kE4m3 ? 128 : 1];
-  // per key of a tile: factor of its scores, value scale over 2^k (twice, as f16);
-  // per tile: k, 2^-k
-  __shared__ __align__(16) float s_scl[kE4m3 ? 2 : 1][2][kE4m3 ? 128 : 4];
-  __shared__ float s_k[2][2];
 
   // barriers and tensor memory need nothing of the kernel before
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -364,19 +528,28 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
           v[e] = in ? v4[e] : 0.f;
           if (v[e] < INFINITY) most = max(most, __float_as_uint(fmaxf(v[e], 0.f)));
         }
-        // the largest scale becomes 64 to 128: times 448 it is below f16's 65504
-        const int k = max((int)(__reduce_max_sync(0xffffffffu, most) >> 23) - 133, -64);
-        const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (scales that are not finite: not this far)
-          const float s = fmaxf(fminf(v[e] * down, 128.f), 0.f);
-          v[e] = __uint_as_float(pack_f16(s, s));
-        }
         float* const at = &s_scl[kE4m3 ? x : 0][0][kE4m3 ? 4 * lane : 0];
         *reinterpret_cast<float4*>(at) = make_float4(a[0], a[1], a[2], a[3]);
-        *reinterpret_cast<float4*>(at + (kE4m3 ? 128 : 0)) = make_float4(v[0], v[1], v[2], v[3]);
-        if (lane < 2) s_k[x][lane] = lane ? down : (float)k;
+        // the largest scale becomes 64 to 128: times 448 it is below f16's 65504
+        int k = max((int)(__reduce_max_sync(0xffffffffu, most) >> 23) - 133, -64);
+        float down = __uint_as_float((uint32_t)(127 - k) << 23);
+        // Drafted rows' scales must not reach the rows that do not see them, as they
+        // would through k: a tile with such rows keeps its values as they are (f16 holds
+        // e4m3) and every scale in its key's exponent.
+        if ((tile + 1) * 128 > w.start) {
+          slow_factors(at, make_float4(v[0], v[1], v[2], v[3]));
+          k = 0;
+          down = 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // (scales that are not finite: not this far)
+            const float s = fmaxf(fminf(v[e] * down, 128.f), 0.f);
+            v[e] = __uint_as_float(pack_f16(s, s));
+          }
+          *reinterpret_cast<float4*>(at + (kE4m3 ? 128 : 0)) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (lane < 2) sh.k[x][lane] = lane ? down : (float)k;
         mbar_arrive_warp(&scl_full[x]);
         key_scales4(p.c, w, key + 128, page, &sk, &sv);
         page = key_page(p.c, w, key + 256);
@@ -386,17 +559,16 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
     // ------------------------------------------------------------ softmax
     const int h = warp >> 2;  // key half
     const int tq = tid & 127;
-    const int part = tq / kRows, row = tq & (kRows - 1);  // part: warp-uniform
+    const int row = tq & (kRows - 1);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tO = tmem + C::kColO + C::D * h + lane_off;
     // After a wait that gave up, a warp still passes every barrier of its piece
     // (the others may be waiting there); the piece's last barrier stops all.
     bool ok = true;
     int n = 0;
     while (walk.next(w)) {
       // ---- Q of the unit, kRep times: 16 (D = 64: 8) lanes per row
-      if (tid < 32) bad[tid] = 0u;
-      if (tid == 0) any_bad = 0;
+      if (tid < 32) sh.bad[tid] = 0u;
+      if (tid == 0) sh.any_bad = 0;
       {
         // The loops are not unrolled: these are a call's first instructions, and
         // fetching them takes longer than the loads.
@@ -448,110 +620,32 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (tid == 0) mbar_arrive(&q_full);
       const float rowf = kE4m3 ? s_rowf[kE4m3 ? tq : 0] : 1.f;
-      const bool used = base + row < w.rows;
-      const int token = used ? row_token(p, w.rt * kUnit + base + row) : 0;
+      const int token = base + row < w.rows ? row_token(p, w.rt * kUnit + base + row) : -1;
 
       float m = -INFINITY, l = 0.f;
       for (int tile = w.t0; tile < w.t1; ++tile, ++n) {
         const int x = n & 1;
-        const uint32_t tS = tmem + C::kColS + 128 * x + 64 * h + lane_off;
+        bool slow = false;
+        if (kE4m3) {  // (there long before the scores)
+          ok = cache_wait_warp(&scl_full[x], (n >> 1) & 1, &abort_flag, p.status, 2523);
+          slow = sh.k[x][1] == 0.f;
+        }
         // (the phase stays until S(n + kKStages), behind this tile's P)
-        ok = cache_wait_warp(&k_empty[n % C::kKStages], (n / C::kKStages) & 1, &abort_flag, p.status,
-                             2521 + h);
-        if (kE4m3 && ok) ok = cache_wait_warp(&scl_full[x], (n >> 1) & 1, &abort_flag, p.status, 2523);
+        if (ok)
+          ok = cache_wait_warp(&k_empty[n % C::kKStages], (n / C::kKStages) & 1, &abort_flag, p.status,
+                               2521 + h);
         if (!ok) break;
-        tc_fence_after();
-        uint32_t r[kKeys];
-        if constexpr (kKeys == 64) FA_TMEM_LD64_SYNC(tS, r);
-        if constexpr (kKeys == 32) FA_TMEM_LD32_SYNC(tS + 32 * part, r);
-        if constexpr (kKeys == 16) FA_TMEM_LD16_SYNC(tS + 16 * part, r);
-        const int koff = 64 * h + kKeys * part;  // the thread's keys in the tile
-        if constexpr (kE4m3) {
-#pragma unroll
-          for (int g = 0; g < kKeys; g += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(&s_scl[kE4m3 ? x : 0][0][koff + g]);
-            const float2 t0 = mul2(make_float2(__uint_as_float(r[g]), __uint_as_float(r[g + 1])),
-                                   make_float2(a.x, a.y));
-            const float2 t1 = mul2(make_float2(__uint_as_float(r[g + 2]), __uint_as_float(r[g + 3])),
-                                   make_float2(a.z, a.w));
-            r[g] = __float_as_uint(t0.x);
-            r[g + 1] = __float_as_uint(t0.y);
-            r[g + 2] = __float_as_uint(t1.x);
-            r[g + 3] = __float_as_uint(t1.y);
-          }
+        if (slow) {
+          const RowState y = slow_tile<C, kRep>(p, w.b, w.start, w.klen, tile == w.t0, sh, smem, tile, n,
+                                                tmem, rowf, token, m, l);
+          m = y.m;
+          l = y.l;
+          ok = y.ok;
+        } else {
+          ok = tile_step<C, kE4m3, kRep, false>(p, w.b, w.start, w.klen, tile == w.t0, sh, smem, tile, n, tmem,
+                                                rowf, token, m, l);
         }
-        if ((tile + 1) * 128 > w.start) {  // drafted rows, and the sequence's end
-          const uint64_t vis = used ? visible_keys<kKeys>(p, w, token, tile * 128 + koff) : ~0ull;
-#pragma unroll
-          for (int e = 0; e < kKeys; ++e)
-            if (!((vis >> e) & 1)) r[e] = 0xff800000u;
-          const int st = kE4m3 ? x : n % C::kVStages;
-          ok = kE4m3 ? cache_wait_warp(&v16_full[x], (n >> 1) & 1, &abort_flag, p.status, 2524)
-                     : cache_wait_warp(&v_full[st], (n / C::kVStages) & 1, &abort_flag, p.status, 2524);
-          if (!ok) break;
-          const int row0 = 64 * h + 16 * (warp & 3);
-          if (tile * 128 + row0 + 16 > w.start)
-            clean_rows<C, false, kE4m3>(
-                smem + (kE4m3 ? C::kOffV16 + st * C::kV16Bytes : C::kOffV + st * C::kTileBytes), w.start,
-                w.klen, row0, row0 + 16, tile * 128, bad, &any_bad);
-        }
-        // the scale (positive) multiplies in the exponent; e4m3: the row's factor
-        const float exp_scale = kE4m3 ? rowf : p.scale_log2;
-        const float k = kE4m3 ? s_k[x][0] : 0.f, down = kE4m3 ? s_k[x][1] : 1.f;
-        float tmax = __uint_as_float(r[0]);
-        if constexpr (kKeys == 64) tmax = fmaxf(max32(r), max32(r + 32));
-        if constexpr (kKeys == 32) tmax = max32(r);
-        if constexpr (kKeys == 16) {
-#pragma unroll
-          for (int e = 1; e < 15; e += 2)
-            tmax = max3(tmax, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-          tmax = fmaxf(tmax, __uint_as_float(r[15]));
-        }
-        const float top = tmax * exp_scale + (k - C::kTop);
-        const bool grow = top > m + C::kGrow;  // true when m = -inf, top finite
-        float alpha = 1.f;
-        if (grow) {
-          alpha = (m == -INFINITY) ? 0.f : ex2(m - top);
-          m = top;
-        }
-        if (tile > w.t0 && __any_sync(0xffffffffu, grow)) {
-          // O_h holds the tiles before this one once the last P_h V is done
-          ok = cache_wait_warp(&pv_done[h][x ^ 1], ((n - 1) >> 1) & 1, &abort_flag, p.status, 2525 + h);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < C::D / 32; ++c) {
-            uint32_t o[32];
-            FA_TMEM_LD32_SYNC(tO + 32 * c, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            FA_TMEM_ST32(tO + 32 * c, o);
-          }
-        }
-        const float nm = (m == -INFINITY) ? 0.f : k - m;
-        const float2 c2 = make_float2(exp_scale, exp_scale), nm2 = make_float2(nm, nm);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // P rounded to bf16 (2^-8 of each weight), as in the forward kernels, or f16;
-        // signalling its first half early, as the d = 128 forward does, gained nothing here
-        uint32_t pk[kKeys / 2];
-#pragma unroll
-        for (int e = 0; e < kKeys; e += 4) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 s = make_float2(__uint_as_float(r[e + 2 * i]), __uint_as_float(r[e + 2 * i + 1]));
-            const float2 t = fma2(s, c2, nm2);
-            const float2 pv = make_float2(ex2(t.x), ex2(t.y));
-            acc[i] = add2(acc[i], pv);
-            pk[e / 2 + i] = kE4m3 ? pack_f16(pv.x, pv.y) : pack_bf16(pv.x, pv.y);
-          }
-        }
-        store_part<kKeys / 2, kRep>(tS, pk, part);
-        const float2 sum = add2(acc[0], acc[1]);
-        l = l * alpha + (sum.x + sum.y) * down;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive_warp(&p_full[x][h]);
-        if (kE4m3 && lane == 0) mbar_arrive(&scl_empty[x]);
+        if (!ok) break;
       }
 
       // ---- epilogue: join the two key halves and the lane blocks
@@ -629,11 +723,11 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
           asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
         }
         if (write) {
-          if (any_bad) {
+          if (sh.any_bad) {
             float extra[kCols];
 #pragma unroll
             for (int e = 0; e < kCols; ++e) extra[e] = 0.f;
-            add_nonfinite<kE4m3>(p, w.b, w.h, w.start, bad, t, col + cg, kCols, extra);
+            add_nonfinite<kE4m3>(p, w.b, w.h, w.start, sh.bad, t, col + cg, kCols, extra);
 #pragma unroll
             for (int e = 0; e < kCols; ++e) v[e] += extra[e];
           }

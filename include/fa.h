@@ -436,7 +436,8 @@ size_t fa_cache_fwd_workspace_size(int B, int Hq, int Hkv, int T, int d);
  *   row's largest are off by up to 2^-21 of that, larger ones are exact.  With G = Hq /
  *   heads and T*G <= 16 a weight is rounded by 2^-8 of itself, or by 2^-30 of the row's
  *   largest weight times value scale.  With T*G > 16, values carry an absolute error of
- *   2^-40 of the largest within the 128 rows from a multiple of 128 on.
+ *   2^-40 of the largest within the 128 rows from a multiple of 128 on that the sequence
+ *   held before these tokens.
  * Limits: T <= 1024; Hq a multiple of cache->heads; B*Hq <= 65535; with G = Hq /
  * heads, B * heads * ceil(T*G / 32) * ceil(capacity / 128) below 2^31. */
 fa_status fa_cache_fwd(const void* q, const fa_cache* cache, const int32_t* start,

@@ -103,3 +103,41 @@ def test_queries_of_uneven_channels(fa, d, T, G, ratio):
         tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * ds[:, None] + 2.0 ** -18) * mag + 2.0 ** -16 * mag
         err = (o[0, :, t].cpu().to(F64) - want).abs()
         assert (err <= tol).all(), (float((err / mag).max()), float((err / tol).max()))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,T,G", [(128, 6, 2), (128, 6, 4), (64, 12, 4), (128, 30, 3), (64, 60, 4)])
+@pytest.mark.parametrize("start", [0, 300, 384])
+def test_large_hidden_values_stay_hidden(fa, fmt, d, T, G, start):
+    """A drafted row whose value scale (bf16: values) is far above the others' changes nothing
+    for the tokens that do not see it, bit for bit."""
+    c = ref.Cache(fa, 1, 400 + T, 1, d, 32, fmt, seed=63)
+    g = torch.Generator().manual_seed(64)
+    q = torch.randn(1, G, T, d, generator=g).to(torch.bfloat16).cuda()
+    u = T // 2
+    sees = torch.ones(T, T).tril().bool()
+    sees[:, u] = torch.arange(T) % 3 == u % 3
+    sees[u, u] = True
+    bits = torch.zeros(1, T, -(-T // 32) * 32, dtype=torch.int64)
+    bits[0, :, :T] = sees
+    words = (bits.view(1, T, -1, 32) << torch.arange(32)).sum(-1)
+    mask = torch.where(words >= 1 << 31, words - (1 << 32), words).int().cuda()
+    st = torch.tensor([start], dtype=torch.int32)
+    call = lambda: [x.clone() for x in fa.cache_forward(q, c.fa, st.cuda(), tree_mask=mask)]
+    o0, l0 = call()
+    p, i = c.where(0, start + u)
+    blind = ~sees[:, u]
+    for shift in (4, 20, 32, 40, 60):
+        old = (c.v[p, 0, i].clone(), None if c.vs is None else c.vs[p, 0, i].clone())
+        if fmt == "e4m3":
+            c.vs[p, 0, i] *= 2.0 ** shift
+        else:
+            c.v[p, 0, i] *= 2.0 ** shift
+        o1, l1 = call()
+        assert torch.equal(l1[0][:, blind], l0[0][:, blind]), shift
+        assert torch.equal(o1[0][:, blind], o0[0][:, blind]), shift
+        ro, rl, to, tl = ref.attend(c, q, st, None, mask, d ** -0.5)
+        assert ((o1.cpu().to(F64) - ro).abs() <= to).all()
+        c.v[p, 0, i] = old[0]
+        if fmt == "e4m3":
+            c.vs[p, 0, i] = old[1]
