@@ -21,9 +21,10 @@
 // e4m3: S from the bytes themselves, Q as an e4m3 and an e5m2 term.  P and V are f16: four more
 // warps scale and convert V on its way, into two buffers of its own.  Its scales are
 // taken relative to 2^k, the power of two below the tile's largest, and 2^k enters the
-// exponents; what that costs is an absolute 2^-40 of the tile's largest value.  (Tiles
-// with drafted rows: each key's scale stands in its own exponent, as in the other
-// kernel, and V is converted as it is.)  A
+// exponents: the values are rounded twice by 2^-11, and a weight that f16 cannot hold is
+// off by 2^-24 of the row's largest (weight times scale).  (Slow tiles, with drafted rows
+// or scales more than 64 times apart: each key's scale stands in its own exponent, as in
+// the other kernel, and V is converted as it is.)  A
 // factor per key that every warp reads costs shared memory a cycle, so the softmax
 // reads one (the score's; in those tiles three): 512 cycles a tile, next to the products' 770, the copies'
 // 256 and the conversion's 384; a tile takes 1900 to 2300.  With P as two e4m3 terms
@@ -127,8 +128,7 @@ struct RowsShared {
   // pv_done[h][x]: O_h has P_h V of buffer x's tile
   uint64_t p_full[2][2], pv_done[2][2], v_full[C::kVStages], v16_full[2], scl_empty[2];
   // per key of a tile: factor of its scores, value scale over 2^k (twice, as f16), and
-  // in a tile whose scales stand in the exponents (2^-k told as 0) their log2 and
-  // inverse; per tile: k, 2^-k
+  // in a slow tile (2^-k told as 0) the scale's log2 and inverse; per tile: k, 2^-k
   __align__(16) float scl[kE4m3 ? 2 : 1][4][kE4m3 ? 128 : 4];
   float k[2][2];
   int abort_flag, any_bad;
@@ -136,8 +136,9 @@ struct RowsShared {
 };
 
 // The softmax of one tile whose scores are there: S(n) to P, m, l and, where m grows,
-// O_h.  token: of this thread's row, negative without one.  kSlow: an e4m3 tile with
-// drafted rows or the sequence's end.  False after a wait that gave up.
+// O_h.  token: of this thread's row, negative without one.  kSlow: an e4m3 tile whose
+// value scales stand in the exponents, all with drafted rows or the sequence's end among
+// them.  False after a wait that gave up.
 template <typename C, bool kE4m3, int kRep, bool kSlow>
 __device__ __forceinline__ bool tile_step(const CacheFwdParams& p, int b, int start, int klen, bool first,
                                           RowsShared<C, kE4m3>& sh, uint8_t* smem, int tile, int n,
@@ -520,23 +521,29 @@ __global__ void __launch_bounds__(CacheRowsCfg<kD, kE4m3>::kThreads, 1)
         const float k4[4] = {sk.x, sk.y, sk.z, sk.w};
         const float v4[4] = {sv.x, sv.y, sv.z, sv.w};
         float a[4], v[4];
-        uint32_t most = 0;
+        uint32_t most = 0, least = 0x7f800000u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool in = key + e < w.klen;  // else: whatever the page holds
           a[e] = in ? k4[e] * p.scale_log2 : 0.f;
           v[e] = in ? v4[e] : 0.f;
-          if (v[e] < INFINITY) most = max(most, __float_as_uint(fmaxf(v[e], 0.f)));
+          const uint32_t bits = __float_as_uint(fmaxf(v[e], 0.f));  // ordered as the values
+          if (v[e] < INFINITY) most = max(most, bits);
+          least = min(least, bits);
         }
+        most = __reduce_max_sync(0xffffffffu, most);
+        least = __reduce_min_sync(0xffffffffu, least);
         float* const at = &s_scl[kE4m3 ? x : 0][0][kE4m3 ? 4 * lane : 0];
         *reinterpret_cast<float4*>(at) = make_float4(a[0], a[1], a[2], a[3]);
         // the largest scale becomes 64 to 128: times 448 it is below f16's 65504
-        int k = max((int)(__reduce_max_sync(0xffffffffu, most) >> 23) - 133, -64);
+        int k = max((int)(most >> 23) - 133, -64);
         float down = __uint_as_float((uint32_t)(127 - k) << 23);
         // Drafted rows' scales must not reach the rows that do not see them, as they
-        // would through k: a tile with such rows keeps its values as they are (f16 holds
-        // e4m3) and every scale in its key's exponent.
-        if ((tile + 1) * 128 > w.start) {
+        // would through k; and where the key of k's scale is not the one that counts, k
+        // would raise the rows' references and push the other tiles' weights below what
+        // f16 holds.  Such tiles keep their values as they are (f16 holds e4m3) and every
+        // scale in its key's exponent.
+        if ((tile + 1) * 128 > w.start || __uint_as_float(most) > 64.f * __uint_as_float(least)) {
           slow_factors(at, make_float4(v[0], v[1], v[2], v[3]));
           k = 0;
           down = 0.f;

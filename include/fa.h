@@ -432,12 +432,12 @@ size_t fa_cache_fwd_workspace_size(int B, int Hq, int Hkv, int T, int d);
  *   rows past it do not exist.
  *   workspace : device, >= fa_cache_fwd_workspace_size bytes, 16-byte aligned;
  *   contents on entry are ignored.
- *   E4M3: scales are finite and not negative.  Elements of q below 2^-13 of their
- *   row's largest are off by up to 2^-21 of that, larger ones are exact.  With G = Hq /
- *   heads and T*G <= 16 a weight is rounded by 2^-8 of itself, or by 2^-30 of the row's
- *   largest weight times value scale.  With T*G > 16, values carry an absolute error of
- *   2^-40 of the largest within the 128 rows from a multiple of 128 on that the sequence
- *   held before these tokens.
+ *   E4M3: scales are finite and not negative; value scales below 2^-64 may count as
+ *   2^-64 (fa_cache_write leaves none).  Elements of q below 2^-13 of their row's largest
+ *   are off by up to 2^-21 of that, larger ones are exact.  With G = Hq / heads and T*G
+ *   <= 16 a weight is rounded by 2^-8 of itself, or by 2^-30 of the row's largest weight
+ *   times value scale; with more, by 2^-11, or 2^-24 of that product, and a value by
+ *   2^-10.
  * Limits: T <= 1024; Hq a multiple of cache->heads; B*Hq <= 65535; with G = Hq /
  * heads, B * heads * ceil(T*G / 32) * ceil(capacity / 128) below 2^31. */
 fa_status fa_cache_fwd(const void* q, const fa_cache* cache, const int32_t* start,

@@ -141,3 +141,43 @@ def test_large_hidden_values_stay_hidden(fa, fmt, d, T, G, start):
         c.v[p, 0, i] = old[0]
         if fmt == "e4m3":
             c.vs[p, 0, i] = old[1]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 8), (1, 24), (1, 60), (1, 128), (2, 100)])
+@pytest.mark.parametrize("shift", [5, 7, 16, 36])
+def test_a_large_value_scale_of_a_weak_key(fa, d, T, G, shift):
+    """A key of the first tile whose weight is next to nothing has a value scale 2^shift above the
+    others: the keys of the other tiles keep their values.  A weight may be 2^-24 of the row's
+    largest (weight times value scale) off, beside its rounding; a value 2^-10 of itself."""
+    n = 700
+    c = ref.Cache(fa, 1, n + T, 1, d, 64, "e4m3", seed=65)
+    c.vs.fill_(1.0 / 64)
+    c.ks.fill_(1.0 / 60)
+    p0, i0 = c.where(0, 17)
+    c.k[..., 3] = 0.0
+    c.k[p0, 0, i0] = 0.0
+    c.k[p0, 0, i0, 3] = -448.0
+    c.vs[p0, 0, i0] *= 2.0 ** shift
+    g = torch.Generator().manual_seed(66)
+    q = torch.randn(1, G, T, d, generator=g)
+    q[..., 3] = 10.0 * (d / 64) ** 0.5       # that key's score: -9.3, in 60ths of 448
+    q = q.to(torch.bfloat16).cuda()
+    if shift > 20:
+        c.ks[p0, 0, i0] *= 6.0               # -56: 2^-81 of the others' weight
+    o, lse = fa.cache_forward(q, c.fa, torch.tensor([n], dtype=torch.int32).cuda())
+    raw = c.raw()
+    k, _ = c.rows(raw, 0, 0, 0, n + T)
+    v, sv = c.rows(raw, 1, 0, 0, n + T)
+    k, v, sv = k[0], v[0], sv[0]
+    for t in range(T):
+        m = n + t + 1
+        kk, vv, qq = k[:m], v[:m], q[0, :, t].cpu().to(F64)
+        p = (qq @ kk.T * d ** -0.5).softmax(-1)
+        want, mag = p @ vv, p @ vv.abs()
+        ds = 2.0 ** -21 * (qq.abs() @ kk.abs().T).amax(-1)
+        top = (p * sv[:m]).amax(-1)
+        tol = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10 + 2 * ds[:, None] + 2.0 ** -18) * mag
+               + 2.0 ** -24 * top[:, None] * (vv.abs() / sv[:m, None]).sum(0))
+        err = (o[0, :, t].cpu().to(F64) - want).abs()
+        assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
