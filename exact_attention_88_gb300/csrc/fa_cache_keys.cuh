@@ -22,7 +22,7 @@
 // thread's maximum: it stays until some score passes it by kGrow (one vote per
 // tile), and only then are the rows' maxima formed (warp reductions, joined in
 // shared memory), the references raised and the accumulator's columns rescaled.  A
-// row that has seen no key yet has reference -1e30 (kept negated): its first
+// row that has seen no key yet has reference -2^128 (kept negated): its first
 // visible key raises it.
 // P goes to shared memory (keys contiguous: the B operand), one element (e4m3: three
 // terms, two keys' bytes of each) per thread and row.
@@ -84,7 +84,9 @@ struct CacheKeysCfg : CacheTile<kD, kE4m3> {
   static_assert(kN * kG <= 128 && 2 * kNO * kG <= 384 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "");
 };
 
-constexpr float kUnset = 1e30f;  // negated reference of a row that has seen no key
+// negated reference of a row that has seen no key: the largest float, so that every
+// score raises it
+constexpr float kUnset = 0x1.fffffep127f;
 
 __device__ __forceinline__ float warp_max(float x) {
   float y;

@@ -439,7 +439,8 @@ size_t fa_cache_fwd_workspace_size(int B, int Hq, int Hkv, int T, int d);
  *   times value scale; with more, by 2^-11, or 2^-24 of that product, and a value by
  *   2^-10.
  * Limits: T <= 1024; Hq a multiple of cache->heads; B*Hq <= 65535; with G = Hq /
- * heads, B * heads * ceil(T*G / 32) * ceil(capacity / 128) below 2^31. */
+ * heads, B * heads * ceil(T*G / 32) * ceil(capacity / 128) below 2^31; with T*G > 32
+ * (E4M3: 16) scores, scale q k, below 2^24 in magnitude. */
 fa_status fa_cache_fwd(const void* q, const fa_cache* cache, const int32_t* start,
                        const int32_t* q_len, const uint32_t* tree_mask, void* o, float* lse,
                        void* workspace, size_t workspace_bytes, int B, int Hq, int T, float scale,

@@ -181,3 +181,25 @@ def test_a_large_value_scale_of_a_weak_key(fa, d, T, G, shift):
                + 2.0 ** -24 * top[:, None] * (vv.abs() / sv[:m, None]).sum(0))
         err = (o[0, :, t].cpu().to(F64) - want).abs()
         assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 12])
+def test_scores_far_below_zero(fa, fmt, G):
+    """Scores of -2e30 and lower are scores like any other: equal ones share the weight."""
+    c = ref.Cache(fa, 1, 400, 1, 64, 32, fmt, seed=67)
+    c.k.zero_()
+    c.k[..., 0] = -448.0
+    if fmt == "e4m3":
+        c.ks.fill_(1.0)
+        c.vs.fill_(0.01)
+    q = torch.zeros(1, G, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** 100
+    n = 300
+    for scale in (0.125, 2.0 ** 10):           # -7.1e31, -5.8e35
+        o, lse = fa.cache_forward(q, c.fa, torch.tensor([n - 1], dtype=torch.int32).cuda(), scale=scale)
+        v, _ = c.rows(c.raw(), 1, 0, 0, n)
+        want, mag = v[0].mean(0), v[0].abs().mean(0)
+        assert ((o[0, :, 0].cpu().to(F64) - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -16) * mag).all()
+        s = -448.0 * 2.0 ** 100 * scale
+        assert ((lse.cpu().to(F64) - s).abs() <= 2.0 ** -21 * abs(s)).all()
