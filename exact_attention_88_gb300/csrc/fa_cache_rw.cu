@@ -123,18 +123,29 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const RwParams
     if constexpr (kE4m3) {
       float amax = row_max<S>(x);
       // infinities out of the scale (rare: the vote keeps the shuffles whole)
-      if (__any_sync(0xffffffffu, !(amax < INFINITY))) {
+      const bool inf = __any_sync(0xffffffffu, !(amax < INFINITY));
+      if (inf) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] : 0.f;
         amax = row_max<S>(x);
         value();
       }
-      const float scale = fmaxf(amax * (1.f / kE4m3Max), kMinScale);
+      // Both divisions, exact to the last bit, are products with an inverse and its rest
+      // (23 K tokens of 8 heads take 33.8 us; with a division each 47; with the inverse
+      // alone 33.2, 59 % of the scales in the last bit and a byte in a thousand a step off).
+      constexpr float kInv = 1.f / kE4m3Max, kInvRest = (float)(1.0 / kE4m3Max - kInv);
+      const float scale = fmaxf(fmaf(amax, kInv, amax * kInvRest), kMinScale);
+      if (inf) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (fabsf(x[e]) == INFINITY) x[e] = copysignf(kE4m3Max * scale, x[e]);
+      }
       if (mine) {
-        const float up = __fdividef(1.f, scale);  // 2^-22, next to a rounding of 2^-4
+        const float up = __fdividef(1.f, scale), rest = fmaf(-up, scale, 1.f) * up;
+        const float2 up2 = make_float2(up, up), rest2 = make_float2(rest, rest);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          const float2 y = mul2(make_float2(x[e], x[e + 1]), make_float2(up, up));
+          const float2 v = make_float2(x[e], x[e + 1]), y = fma2(v, up2, mul2(v, rest2));
           x[e] = y.x;
           x[e + 1] = y.y;
         }

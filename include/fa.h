@@ -395,7 +395,7 @@ typedef struct {
  * row of the cache changes.  With `rotary`, k is rotated first (fp32, not
  * rounded in between); rotary->pos NULL means the cache row.
  * E4M3: scale = max over the row's finite |x| / 448, at least 2^-64, and the
- * value is x / scale rounded to nearest (ties to even); infinities become
+ * value is x / scale (both fp32 quotients) rounded to nearest (ties to even); infinities become
  * +-448, NaN stays NaN.
  *   start, q_len : device int32 [B]; q_len NULL: T for every sequence.  q_len
  *   is clamped to 0..T; a row outside the sequence's capacity is not written,
