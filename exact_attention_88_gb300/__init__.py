@@ -633,7 +633,19 @@ def rope_frequencies(dim, base=10000.0, scaling="none", factor=1.0, original=409
     return f.to(device), attention
 
 
-class Rope:
+class _Fixed:
+    """Attributes are set once: the calls use pointers and sizes taken when the object is made."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError("a %s's %s is fixed: make another" % (type(self).__name__, name))
+        self.__dict__[name] = value
+
+    def __delattr__(self, name):
+        raise AttributeError("a %s's %s is fixed" % (type(self).__name__, name))
+
+
+class Rope(_Fixed):
     """Rotary positions: `freq`, a CUDA float64 tensor of dim / 2 radians per
     position (rope_frequencies), pairs (2p, 2p + 1) when interleaved, else
     (p, p + dim / 2), and a factor on the rotated elements."""
@@ -722,12 +734,13 @@ def rope_backward(dq, dk, rope, positions=None, out=None, stream=None):
         return _rope(lib.fa_rope_bwd, lib.fa_rope_bwd_fp32, dq, dk, rope, positions, out)
 
 
-class KVCache:
+class KVCache(_Fixed):
     """A key/value cache (fa_cache) over the caller's CUDA tensors: k, v
     [pages, heads, page_size, d] (bf16, or float8_e4m3fn with fp32 scales
     [pages, heads, page_size]), and block_table, int32 [B, width] (None:
     sequence b owns page b).  The tensors are kept, and read and written where
-    they are; the block table's contents may change between calls."""
+    they are; their contents, the block table's too, may change between calls, the
+    attributes may not."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, block_table=None):
         import torch
