@@ -757,14 +757,14 @@ class KVCache(_Fixed):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.block_table = block_table
         pages, heads, page, d = k.shape
-        self._layout, self._scale_layout = layout_of(k), None
+        scale_layout = None
         if e4m3:
             for s in (k_scale, v_scale):
                 if (s.dtype != torch.float32 or s.shape != k.shape[:3]
                         or s.stride() != k_scale.stride() or (page > 1 and s.stride(2) != 1)):
                     raise ValueError("scales must be fp32 [pages, heads, page_size] with "
                                      "contiguous rows")
-            self._scale_layout = FaLayout(k_scale.stride(0), k_scale.stride(1), 1)
+            scale_layout = FaLayout(k_scale.stride(0), k_scale.stride(1), 1)
         width, stride = 0, 0
         if block_table is not None:
             if (block_table.dim() != 2 or block_table.dtype != torch.int32
@@ -776,10 +776,11 @@ class KVCache(_Fixed):
         self.heads, self.d, self.device = heads, d, k.device
         self.sequences = pages if block_table is None else block_table.shape[0]
         self.capacity = page if block_table is None else width * page
+        self._layout, self._scale_layout = layout_of(k), scale_layout
         self.struct = FaCache(
             self.format, pages, page, heads, d, k.data_ptr(), v.data_ptr(), _ptr(k_scale),
             _ptr(v_scale), ctypes.pointer(self._layout),
-            ctypes.pointer(self._scale_layout) if e4m3 else None, _ptr(block_table), width, stride)
+            ctypes.pointer(scale_layout) if e4m3 else None, _ptr(block_table), width, stride)
 
     @classmethod
     def empty(cls, pages, page_size, heads, d, dtype, block_table=None, device="cuda"):
