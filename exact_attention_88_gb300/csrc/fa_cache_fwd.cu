@@ -4,9 +4,10 @@
 namespace fa {
 
 size_t cache_fwd_workspace(int B, int Hq, int Hkv, int T, int d) {
-  // two partial results per CTA: the first and the last unit of its run
+  // two partial results per run: its first and its last unit (256 rows: two CTAs to a run)
   const int rows = cache_fwd_rows(T * (Hq / Hkv));
-  return (size_t)2 * kCacheMaxCtas * rows * (d + 2) * sizeof(float);
+  const int runs = rows == 256 ? kCacheMaxCtas / 2 : kCacheMaxCtas;
+  return (size_t)2 * runs * rows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_cache_fwd(const CacheFwdArgs& a, cudaStream_t s) {

@@ -41,3 +41,10 @@ def test_rope_attributes_are_fixed(fa):
         with pytest.raises(AttributeError):
             delattr(r, name)
     assert (r.dim, r.interleaved, r.factor) == (32, False, 1.0)
+
+
+def test_workspace_of_paired_ctas(fa):
+    # 129 to 256 rows: two CTAs share a run, so there are as many partial rows as at 128
+    f = fa.fa_cache_fwd_workspace_size
+    for d in (64, 128):
+        assert f(1, 8, 1, 1024, d) == f(3, 2, 1, 70, d) == f(1, 8, 1, 16, d) == 2 * f(1, 8, 1, 8, d)
