@@ -624,6 +624,8 @@ def rope_frequencies(dim, base=10000.0, scaling="none", factor=1.0, original=409
     if scaling == "linear":
         f = f / factor
     elif scaling == "bands":
+        if not slow_turns < fast_turns:
+            raise ValueError('"bands" scaling needs slow_turns < fast_turns')
         turns = original * f / (2.0 * math.pi)
         keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0.0, 1.0)
         f = f * keep + f / factor * (1.0 - keep)

@@ -48,3 +48,10 @@ def test_workspace_of_paired_ctas(fa):
     f = fa.fa_cache_fwd_workspace_size
     for d in (64, 128):
         assert f(1, 8, 1, 1024, d) == f(3, 2, 1, 70, d) == f(1, 8, 1, 16, d) == 2 * f(1, 8, 1, 8, d)
+
+
+def test_bands_without_a_ramp_are_refused(fa):
+    # (equal ends would make 0 / 0 of a pair that turns just as often)
+    for slow, fast in ((8.0, 8.0), (9.0, 8.0), (float("nan"), 8.0)):
+        with pytest.raises(ValueError):
+            fa.rope_frequencies(64, scaling="bands", factor=4.0, slow_turns=slow, fast_turns=fast, device="cpu")
