@@ -588,17 +588,38 @@ __device__ __noinline__ void add_nonfinite(const CacheFwdParams& p, int b, int h
     }
 }
 
-// Makes V rows of a tile that reaches past start[b] safe to multiply by zero: rows
-// [row0, row1) of the tile, by this warp.  Rows behind the sequence become zero;
+// Makes V rows of a tile that reaches past start[b] safe to multiply by zero: kRows rows
+// of the tile from row0 on, by this warp.  Rows behind the sequence become zero;
 // non-finite elements of drafted rows too, and the rows are flagged.  The tile is of
-// bf16, or f16 converted from e4m3 (kF16), or (kBytes) e4m3 itself.
-template <typename C, bool kBytes, bool kF16 = false>
-__device__ __noinline__ void clean_rows(uint8_t* tile, int start, int klen, int row0, int row1,
-                                        int key_base, uint32_t* bad, int* any_bad) {
+// bf16, or f16 converted from e4m3 (kF16), or (kBytes) e4m3 itself.  Where no row is
+// behind the sequence a look without branches mostly finds that there is nothing to do
+// (1024 tokens over an empty e4m3 cache 82 -> 68 us, bf16 50 -> 38; unrolled further 67
+// and 36, but then the code that the main loops share a cache with makes them 2 % slower).
+template <typename C, int kRows, bool kBytes, bool kF16 = false>
+__device__ __noinline__ void clean_rows(uint8_t* tile, int start, int klen, int row0, int key_base,
+                                        uint32_t* bad, int* any_bad) {
   constexpr int kChunkRow = kF16 ? 128 : C::kChunkRow, kChunks = kF16 ? C::D / 64 : C::kChunks;
   constexpr int kPieces = kChunkRow / 16;  // 16-byte pieces of a chunk's row
-  constexpr uint32_t kAll = kF16 ? 0x7c007c00u : 0x7f807f80u;
-  const int first = max(row0, start - key_base);
+  // all-ones exponent fields (bf16: 8 bits, f16: 5; e4m3's NaN: 7 bits); one more
+  // there carries into the sign's place
+  constexpr uint32_t kAll = kBytes ? 0x7f7f7f7fu : kF16 ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t kOne = kBytes ? 0x01010101u : kF16 ? 0x04000400u : 0x00800080u;
+  const int first = max(row0, start - key_base), row1 = row0 + kRows;
+  if (key_base + row1 <= klen) {
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int c = 0; c < kChunks; ++c) {
+      const uint4* const at = reinterpret_cast<const uint4*>(tile + c * 128 * kChunkRow);
+#pragma unroll 2
+      for (int j = 0; j < kRows * kPieces / 32; ++j) {
+        const int i = row0 * kPieces + 32 * j + (threadIdx.x & 31);
+        if (i < first * kPieces) continue;
+        const uint4 v = at[i];
+        found |= ((v.x & kAll) + kOne) | ((v.y & kAll) + kOne) | ((v.z & kAll) + kOne) | ((v.w & kAll) + kOne);
+      }
+    }
+    if (!__any_sync(0xffffffffu, found & (kBytes ? 0x80808080u : 0x80008000u))) return;
+  }
 #pragma unroll 1
   for (int c = 0; c < kChunks; ++c) {
     uint4* const at = reinterpret_cast<uint4*>(tile + c * 128 * kChunkRow);
@@ -612,9 +633,7 @@ __device__ __noinline__ void clean_rows(uint8_t* tile, int start, int klen, int 
         uint32_t found = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          // all-ones exponent fields (bf16: 8 bits, f16: 5; e4m3's NaN: 7 bits)
-          const uint32_t m = kBytes ? __vcmpeq4(x[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                                    : __vcmpeq2(x[k] & kAll, kAll);
+          const uint32_t m = kBytes ? __vcmpeq4(x[k] & kAll, kAll) : __vcmpeq2(x[k] & kAll, kAll);
           found |= m;
           x[k] &= ~m;
         }

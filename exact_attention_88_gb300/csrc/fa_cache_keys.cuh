@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(CacheKeysCfg<kD, kE4m3, kR>::kThreads, 1)
                 if (!((sees >> r) & 1u)) t[r] = -INFINITY;
             }
             if (tile * 128 + 32 * wq + 32 > w.start)
-              clean_rows<C, kE4m3>(smem + C::kOffV + (n % C::kVStages) * C::kTileBytes, w.start, w.klen,
-                                   32 * wq, 32 * wq + 32, tile * 128, bad[y], &any_bad[y]);
+              clean_rows<C, 32, kE4m3>(smem + C::kOffV + (n % C::kVStages) * C::kTileBytes, w.start,
+                                       w.klen, 32 * wq, tile * 128, bad[y], &any_bad[y]);
           }
         } else {
 #pragma unroll

@@ -183,9 +183,9 @@ __device__ __forceinline__ bool tile_step(const CacheFwdParams& p, int b, int st
     if (!ok) return false;
     const int row0 = 64 * h + 16 * (warp & 3);
     if (tile * 128 + row0 + 16 > start)
-      clean_rows<C, false, kE4m3>(
+      clean_rows<C, 16, false, kE4m3>(
           smem + (kE4m3 ? C::kOffV16 + st * C::kV16Bytes : C::kOffV + st * C::kTileBytes), start, klen,
-          row0, row0 + 16, tile * 128, sh.bad, &sh.any_bad);
+          row0, tile * 128, sh.bad, &sh.any_bad);
   }
   // the scale (positive) multiplies in the exponent; e4m3: the row's factor
   const float exp_scale = !kE4m3 ? p.scale_log2 : kSlow ? 1.f : rowf;
