@@ -37,9 +37,11 @@ cudaError_t launch_cache_fwd(const CacheFwdArgs& a, cudaStream_t s) {
   if (!encode_cache_map(&m.k, c.k, c.l, c, esize, p.box_rows) ||
       !encode_cache_map(&m.v, c.v, c.l, c, esize, p.box_rows))
     return cudaErrorInvalidValue;
-  // e4m3 units of 17 to 32 rows: P costs the keys kernel two terms per element, the rows
-  // kernel one f16 (16 sequences of 16 K keys, 32 rows: 163 and 132 us at d = 128, 157
-  // and 104 at d = 64); bf16's cost the keys kernel less than its loads
+  // e4m3 units of 17 to 32 rows: P costs the keys kernel three terms per element (of two it
+  // was), the rows kernel one f16 (16 sequences of 16 K keys, 32 rows: 163, with two terms,
+  // and 133 us at d = 128, 157 and 104 at d = 64; of 16 rows: 91 and 98 at d = 64, 64
+  // sequences of up to 8 K keys at d = 128: 160 and 204); bf16's cost the keys kernel less
+  // than its loads
   const bool keys = p.T * p.group <= (c.ks ? 16 : 32);
   p.slack = keys && !c.ks ? 4.f : 5.5f;
   if (!c.ks) return keys ? launch_cache_keys_bf16(m, p, s) : launch_cache_rows_bf16(m, p, s);

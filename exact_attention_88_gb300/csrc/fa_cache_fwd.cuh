@@ -15,12 +15,11 @@
 // e4m3.  S is formed from the cache's 8-bit values (kind::f8f6f4, fp32 accumulation,
 // exact products): Q, scaled by a power of two per row, is the sum of two 8-bit terms,
 // exact down to 2^-13 of the row's largest element, and the keys' scales multiply the
-// scores.  For few
-// query rows P V is too: P as three e5m2 terms keeps 8 to 9 bits, and the values' scales s_v
-// enter the exponent: P' = 2^(s + log2 s_v - m) with m following the maximum of that
-// sum, so that a row's largest *contribution* sits at 2^13 .. 2^15.75 of the terms'
-// range whatever the scales are; l sums P' / s_v.  For more rows P is f16 and V is scaled and
-// converted to f16 on its way.
+// scores.  For few query rows P V is too: P as three e5m2 terms keeps 8 to 9 bits, and
+// the values' scales s_v enter the exponent: P' = 2^(s + log2 s_v - m) with m following
+// the maximum of that sum, so that a row's largest *contribution* sits at 2^13 ..
+// 2^15.75 of the terms' range whatever the scales are; l sums P' / s_v.  For more rows P
+// is f16 and V is scaled and converted to f16 on its way.
 //
 // Rows behind the sequence and drafted tokens that a query row does not see may
 // hold anything, and 0 * NaN is NaN in a matrix product: in the tiles that

@@ -18,19 +18,19 @@
 // A tile takes about 1600 cycles (bf16, 61-token trees: 105 us, 56% of the memory's
 // rate), the chain of a tile's scores, exponentials and products.
 //
-// e4m3: S from the bytes themselves, Q as an e4m3 and an e5m2 term.  P and V are f16: four more
-// warps scale and convert V on its way, into two buffers of its own.  Its scales are
-// taken relative to 2^k, the power of two below the tile's largest, and 2^k enters the
-// exponents: the values are rounded twice by 2^-11, and a weight that f16 cannot hold is
-// off by 2^-24 of the row's largest (weight times scale).  (Slow tiles, with drafted rows
-// or scales more than 64 times apart: each key's scale stands in its own exponent, as in
-// the other kernel, and V is converted as it is.)  A
-// factor per key that every warp reads costs shared memory a cycle, so the softmax
-// reads one (the score's; in those tiles three): 512 cycles a tile, next to the products' 770, the copies'
-// 256 and the conversion's 384; a tile takes 1900 to 2300.  With P as two e4m3 terms
-// and three factors per key (value scales in the exponents) it was 3600.  The loops are
-// kept short: with the conversion and the scales' loop unrolled, warps waited for
-// instructions three times as often as they issued one, and nothing else counted.
+// e4m3: S from the bytes themselves, Q as an e4m3 and an e5m2 term.  P and V are f16:
+// four more warps scale and convert V on its way, into two buffers of its own.  Its
+// scales are taken relative to 2^k, the power of two below the tile's largest, and 2^k
+// enters the exponents: the values are rounded twice by 2^-11, and a weight that f16
+// cannot hold is off by 2^-24 of the row's largest (weight times scale).  A factor per
+// key that every warp reads costs shared memory a cycle, so the softmax reads one (the
+// score's): 512 cycles a tile, next to the products' 770, the copies' 256 and the
+// conversion's 384; a tile takes 1900 to 2300.  With P as two e4m3 terms and three
+// factors per key (value scales in the exponents) it was 3600.  Slow tiles, with drafted
+// rows or scales more than 64 times apart, do read three: each key's scale stands in its
+// own exponent, as in the other kernel, and V is converted as it is.  The loops are kept
+// short: with the conversion and the scales' loop unrolled, warps waited for instructions
+// three times as often as they issued one, and nothing else counted.
 #pragma once
 
 #include "fa_cache_fwd.cuh"
@@ -178,8 +178,9 @@ __device__ __forceinline__ bool tile_step(const CacheFwdParams& p, int b, int st
     for (int e = 0; e < kKeys; ++e)
       if (!((vis >> e) & 1)) r[e] = 0xff800000u;
     const int st = kE4m3 ? x : n % C::kVStages;
-    const bool ok = kE4m3 ? cache_wait_warp(&sh.v16_full[x], (n >> 1) & 1, &sh.abort_flag, p.status, 2524)
-               : cache_wait_warp(&sh.v_full[st], (n / C::kVStages) & 1, &sh.abort_flag, p.status, 2524);
+    const bool ok =
+        kE4m3 ? cache_wait_warp(&sh.v16_full[x], (n >> 1) & 1, &sh.abort_flag, p.status, 2524)
+              : cache_wait_warp(&sh.v_full[st], (n / C::kVStages) & 1, &sh.abort_flag, p.status, 2524);
     if (!ok) return false;
     const int row0 = 64 * h + 16 * (warp & 3);
     if (tile * 128 + row0 + 16 > start)

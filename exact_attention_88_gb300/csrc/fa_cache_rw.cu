@@ -7,10 +7,12 @@
 // reading the rotated bf16 keys.  Both kernels are bound by memory: a bf16 row
 // of 2 d bytes on one side, d + 4 bytes (e4m3) on the other.  d/16 neighbouring
 // lanes hold a row, 16 elements each; a thread keeps its token, its slot and K or
-// V, and steps through the heads, a few of them in flight.  The write of 32 K tokens
-// x 8 heads takes 34 us where the memory needs 21: some 120 instructions per 16
-// elements (rotation, largest magnitude, conversion) issue for about 15 of them.
-// (With the place of every row looked up and divided out anew there were 390.)
+// V, and steps through the heads, a few of them in flight.  The write of 23 K tokens
+// (four prompts of up to 8 K) x 8 heads takes 33.8 us where the memory needs 21.5.
+// Neither the issue (68 %: some 120 instructions per 16 elements) nor the memory
+// (42 %) is full: 27 warps per SM each go through a row's chain of copy, rotation,
+// largest magnitude over the lanes and conversion.  (With the place of every row
+// looked up and divided out anew there were 390 instructions.)
 #include "fa_cache.cuh"
 
 namespace fa {

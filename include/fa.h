@@ -426,12 +426,14 @@ size_t fa_cache_fwd_workspace_size(int B, int Hq, int Hkv, int T, int d);
  * over the rows seen and lse as in fa_fwd; a token that sees nothing gets O = 0
  * and lse = -inf.  Rows t >= q_len[b] of o and lse are left as they were.  What
  * rows that a token does not see hold (infinities and NaN too) never reaches
- * its output.
+ * its output; an infinity among the values that it does see makes it infinite or
+ * NaN.
  *   q, o : [B,Hq,T,d] bf16 (lq, lo NULL: dense).   lse : fp32 [B,Hq,T].
  *   start, q_len : as in fa_cache_write; start is clamped to the capacity, and
  *   rows past it do not exist.
  *   workspace : device, >= fa_cache_fwd_workspace_size bytes, 16-byte aligned;
- *   contents on entry are ignored.
+ *   contents on entry are ignored.  Calls that may run at the same time (on two
+ *   streams, or two graphs) need one each.
  *   E4M3: scales are finite and not negative; value scales below 2^-64 may count as
  *   2^-64 (fa_cache_write leaves none).  Elements of q below 2^-13 of their row's largest
  *   are off by up to 2^-21 of that, larger ones are exact.  With G = Hq / heads and T*G
