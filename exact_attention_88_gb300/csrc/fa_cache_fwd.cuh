@@ -301,7 +301,8 @@ __device__ __forceinline__ void mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64
 // Instruction descriptor, kind::f8f6f4 with A and B e4m3 (format 0; a5, b5: e5m2), D fp32.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn, bool a5 = false,
                                                   bool b5 = false) {
-  return (1u << 4) | ((a5 ? 1u : 0u) << 7) | ((b5 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+  return (1u << 4) | ((a5 ? 1u : 0u) << 7) | ((b5 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Instruction descriptor of kind::f16 for f16 x f16 -> fp32.
@@ -514,9 +515,9 @@ __device__ __forceinline__ void split_p(uint32_t x, uint32_t* t) {
 // normal (2^-6 and up); the second term holds it as e5m2, where the terms' products add
 // up in one accumulator, or times 16 as e4m3 (kTimes16), where they are apart.  Either
 // way the sum is exact from 2^-6 up, 2^-13 of the row's largest (224 to 448), and at
-// most 2^-14 off below.  (With a second term of the first's type and scale 2^-10: rows with one
-// channel 1000 times the others lost bits of those.)  A row with infinities or NaN has
-// no finite score: its factor is NaN.  Called by the whole warp.
+// most 2^-14 off below.  (With a second term of the first's type and scale 2^-10: rows
+// with one channel 1000 times the others lost bits of those.)  A row with infinities or
+// NaN has no finite score: its factor is NaN.  Called by the whole warp.
 struct SplitQ {
   uint2 hi, lo;
   float factor;
@@ -614,7 +615,8 @@ __device__ __noinline__ void clean_rows(uint8_t* tile, int start, int klen, int 
         const int i = row0 * kPieces + 32 * j + (threadIdx.x & 31);
         if (i < first * kPieces) continue;
         const uint4 v = at[i];
-        found |= ((v.x & kAll) + kOne) | ((v.y & kAll) + kOne) | ((v.z & kAll) + kOne) | ((v.w & kAll) + kOne);
+        found |= ((v.x & kAll) + kOne) | ((v.y & kAll) + kOne) | ((v.z & kAll) + kOne) |
+                 ((v.w & kAll) + kOne);
       }
     }
     if (!__any_sync(0xffffffffu, found & (kBytes ? 0x80808080u : 0x80008000u))) return;
